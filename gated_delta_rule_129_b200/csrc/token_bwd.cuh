@@ -264,10 +264,12 @@ __global__ void __launch_bounds__(kBwdWarps * 32, pro_bwd_blocks(sizeof(XT), W))
         warp_sums<2 * G>(sums);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const float r = rsqrt_ftz(sums[2 * g] + kTokEps), k = -(r * r * r) * sums[2 * g + 1];
+          // r (dy - y (y . dy)) as r (dy + m s): every factor stays near dy or the row's norm, where
+          // r^3 would leave fp32's range from a norm of 1e12 on
+          const float r = rsqrt_ftz(sums[2 * g] + kTokEps), m = -(r * sums[2 * g + 1]) * r;
 #pragma unroll
           for (int e = 0; e < NP; ++e)
-            du[g][e] = __ffma2_rn(make_float2(k, k), s[g][e], __fmul2_rn(make_float2(r, r), du[g][e]));
+            du[g][e] = __fmul2_rn(make_float2(r, r), __ffma2_rn(make_float2(m, m), s[g][e], du[g][e]));
         }
       }
 #pragma unroll

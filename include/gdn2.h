@@ -400,6 +400,8 @@ GDN2_API gdn2_status gdn2_act_unpack(const int8_t* codes, const uint8_t* exps, l
  * gdn2_token_prologue_bwd_workspace_size(desc, conv_width) bytes, 256-byte
  * aligned.  No output may overlap an input.  Every output is written; the
  * sums over tokens are added in a fixed order, so results repeat bit by bit.
+ * A row's sum of squares (of silu(conv), q and k) has to fit fp32, a norm of
+ * 1.8e19; past it the forward call gives 0 and the gradient is unspecified.
  * cu_seqlens is not validated (as in the forward call: a malformed array gives
  * unspecified outputs, but every access stays inside the buffers).
  * Asynchronous on `stream`.  Errors (before any launch): GDN2_ERR_NULL, _DTYPE,
