@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import threading
 from typing import NamedTuple
@@ -606,14 +607,19 @@ def _on_stream(f):
     """``f`` with a ``stream`` argument: the whole call, its outputs and its
     workspace included, belongs to that stream, so that no block of memory is
     handed out again while the stream still uses it."""
+    lead = next(iter(inspect.signature(f).parameters))   # a tensor or a PackedAct: it says where the call belongs
+
     @functools.wraps(f)
     def call(*args, stream=None, **kw):
         if stream is None:
             return f(*args, **kw)
-        first = args[0] if args else next(iter(kw.values()))
-        first = first[0] if isinstance(first, tuple) else first
-        if first.device != stream.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
+        first = args[0] if args else kw.get(lead)
+        first = first[0] if isinstance(first, (tuple, list)) and first else first
+        device = getattr(first, "device", None)
+        if device is None:
+            return f(*args, **kw)   # which says what is wrong with it
+        if device != stream.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         with _torch().cuda.stream(stream):
             return f(*args, **kw)
     return call

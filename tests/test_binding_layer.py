@@ -1,0 +1,49 @@
+"""The binding's training calls on the CPU: what they hand to the library, and what they refuse.  No kernel runs; where a
+call has to get past its checks, the device check and the library call are stood in for."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import gated_delta_rule_129_b200 as gdn2
+
+
+def _packed(*shape):
+    return gdn2.PackedAct(torch.zeros(shape, dtype=torch.int8), torch.zeros((*shape[:-1], 1), dtype=torch.uint8))
+
+
+def _x(*shape):
+    return torch.zeros(shape)
+
+
+T4 = (1, 4, 2, 64)
+BY_KEYWORD = [
+    ("act_pack", dict(out=None, x=_x(*T4))),
+    ("act_unpack", dict(dtype=torch.float32, packed=_packed(*T4))),
+    ("act_unpack", dict(packed=list(_packed(*T4)))),
+    ("token_prologue_bwd", dict(cu_seqlens=None, conv_q=_x(128, 4), conv_k=_x(128, 4), conv_v=_x(128, 4), dq=_x(*T4),
+                                dk=_x(*T4), dv=_x(*T4), q_raw=_packed(*T4), k_raw=_packed(*T4), v_raw=_packed(*T4))),
+    ("token_epilogue_bwd", dict(workspace=None, o=_packed(*T4), gate=_x(*T4), norm_weight=_x(64), dout=_x(*T4))),
+    ("token_path_bwd", dict(scale=None, h0=None, q_raw=_x(*T4), k_raw=_x(*T4), v_raw=_x(*T4), log_alpha=_x(*T4),
+                            b=_x(*T4), w=_x(*T4), gate=_x(*T4), conv_q=_x(128, 4), conv_k=_x(128, 4),
+                            conv_v=_x(128, 4), norm_weight=_x(64), dout=_x(*T4))),
+    ("gated_scan_fwd", dict(h0=None, v=_x(*T4), log_alpha=_x(*T4), w=_x(*T4))),
+    ("gated_scan_bwd", dict(cu_seqlens=None, dO=_x(*T4), v=_x(*T4), log_alpha=_x(*T4), w=_x(*T4))),
+    ("gated_scan_step", dict(out=None, v=_x(4, 2, 64), log_alpha=_x(4, 2, 64), w=_x(4, 2, 64), state=_x(4, 2, 64))),
+]
+
+
+@pytest.mark.parametrize("name,kw", BY_KEYWORD, ids=[f"{i}-{n}" for i, (n, _) in enumerate(BY_KEYWORD)])
+def test_stream_of_another_device_is_refused_by_keyword_too(name, kw):
+    """The call's device is that of its leading argument, wherever and in whatever order it is given."""
+    stream = SimpleNamespace(device=torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="stream is on"):
+        getattr(gdn2, name)(**kw, stream=stream)
+
+
+def test_a_missing_leading_argument_is_named():
+    stream = SimpleNamespace(device=torch.device("cuda", 0))
+    with pytest.raises(TypeError, match="x"):
+        gdn2.act_pack(stream=stream)
+    with pytest.raises(TypeError, match="v"):
+        gdn2.gated_scan_step(log_alpha=_x(4, 2, 64), w=_x(4, 2, 64), state=_x(4, 2, 64), stream=stream)
