@@ -72,7 +72,7 @@ gdn2_status check_pack(long long rows, int cols, gdn2_io_dtype io, const void* x
     cols = gdn2::kPackCols;
   }
   a->cols = cols;
-  a->blocks = (cols + gdn2::kPackCols - 1) / gdn2::kPackCols;
+  a->blocks = cols / gdn2::kPackCols + (cols % gdn2::kPackCols != 0);   // cols may be near 2^31
   if (rows > (1ll << 62) / a->blocks) return GDN2_ERR_SHAPE;
   a->total = rows * a->blocks;
   *values = io == GDN2_IO_BF16 && cols % 8 == 0 ? 8 : 4;   // a lane's
