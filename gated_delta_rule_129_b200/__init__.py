@@ -681,6 +681,17 @@ def _blocks(d):
     return (d + 127) // 128
 
 
+def _rows_cols(name, t):
+    """``t``'s rows and their length for the library, whose rows are under 2^31
+    values long: rows of whole blocks go as rows of one block, stored alike."""
+    D = t.shape[-1]
+    if D % 128 == 0:
+        return t.numel() // 128, 128
+    if D > 0x7fffffff:
+        raise ValueError(f"{name} has rows of D = {D} values; past 2^31 D must be a multiple of 128")
+    return t.numel() // D, D
+
+
 @_on_stream
 def act_pack(x, *, out=None):
     """``gdn2_act_pack``: ``x`` (float32 or bfloat16 ``[..., D]``) in 8 bits, one
@@ -692,16 +703,15 @@ def act_pack(x, *, out=None):
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"x must have shape [..., D] with D >= 1, got {tuple(x.shape)}")
     _need_contig(x)
-    D = x.shape[-1]
-    eshape = (*x.shape[:-1], _blocks(D))
+    rows, cols = _rows_cols("x", x)
+    eshape = (*x.shape[:-1], _blocks(x.shape[-1]))
     if out is None:
         out = PackedAct(torch.empty_like(x, dtype=torch.int8), torch.empty(eshape, dtype=torch.uint8, device=dev))
     else:
         out = PackedAct(*out)
         _expect("out.codes", out.codes, x.shape, torch.int8, dev)
         _expect("out.exps", out.exps, eshape, torch.uint8, dev)
-    _call("gdn2_act_pack", dev, x.data_ptr(), io, x.numel() // D, D,
-          out.codes.data_ptr(), out.exps.data_ptr())
+    _call("gdn2_act_pack", dev, x.data_ptr(), io, rows, cols, out.codes.data_ptr(), out.exps.data_ptr())
     return out
 
 
@@ -717,14 +727,14 @@ def act_unpack(packed, dtype=None, *, out=None):
     D = codes.shape[-1]
     _expect("codes", codes, codes.shape, torch.int8, dev)
     _expect("exps", exps, (*codes.shape[:-1], _blocks(D)), torch.uint8, dev)
+    rows, cols = _rows_cols("codes", codes)
     dtype = dtype if dtype is not None else torch.bfloat16 if out is None else out.dtype
     io = _io(dtype)
     if out is None:
         out = torch.empty_like(codes, dtype=dtype)
     else:
         _expect("out", out, codes.shape, dtype, dev)
-    _call("gdn2_act_unpack", dev, codes.data_ptr(), exps.data_ptr(),
-          codes.numel() // D, D, io, out.data_ptr())
+    _call("gdn2_act_unpack", dev, codes.data_ptr(), exps.data_ptr(), rows, cols, io, out.data_ptr())
     return out
 
 

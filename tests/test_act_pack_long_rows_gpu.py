@@ -15,7 +15,7 @@ def gdn2(cuda_device):
     return mod
 
 
-@pytest.mark.parametrize("D", [2 ** 31 - 1])
+@pytest.mark.parametrize("D", [2 ** 31 - 1, 2 ** 31 + 128, 2 ** 32 + 128])
 def test_long_rows(gdn2, D):
     import torch
     head = np.random.default_rng(1).standard_normal(256).astype(np.float32)

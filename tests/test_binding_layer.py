@@ -47,3 +47,35 @@ def test_a_missing_leading_argument_is_named():
         gdn2.act_pack(stream=stream)
     with pytest.raises(TypeError, match="v"):
         gdn2.gated_scan_step(log_alpha=_x(4, 2, 64), w=_x(4, 2, 64), state=_x(4, 2, 64), stream=stream)
+
+
+@pytest.mark.parametrize("shape", [(2 ** 32 + 128,), (2 ** 31 + 128,), (3, 2 ** 32 + 256), (2, 5, 128), (7, 1001), (4, 128, 64)])
+def test_checkpoints_describe_every_value(monkeypatch, shape):
+    """Rows and columns that reach the library cover the tensor, however long its rows are."""
+    calls = {}
+    monkeypatch.setattr(gdn2, "_cuda_device", lambda name, t: t.device)
+    monkeypatch.setattr(gdn2, "_call", lambda where, device, *args: calls.update({where: args}))
+    x = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    p = gdn2.act_pack(x)
+    gdn2.act_unpack(p)
+    _, _, rows, cols, _, _ = calls["gdn2_act_pack"]
+    assert calls["gdn2_act_unpack"][2:4] == (rows, cols)
+    assert rows * cols == x.numel() and cols < 2 ** 31
+    assert rows * -(-cols // 128) == p.exps.numel()
+
+
+@pytest.mark.parametrize("D", [2 ** 31, 2 ** 31 + 1, 2 ** 32 + 1])
+def test_checkpoints_refuse_rows_past_the_library(monkeypatch, D):
+    """Odd rows of 2^31 values and more (2^31 itself is whole blocks, and goes through)."""
+    monkeypatch.setattr(gdn2, "_cuda_device", lambda name, t: t.device)
+    monkeypatch.setattr(gdn2, "_call", lambda *a: None)
+    x = torch.empty(2, D, dtype=torch.bfloat16, device="meta")
+    p = gdn2.PackedAct(torch.empty(2, D, dtype=torch.int8, device="meta"),
+                       torch.empty(2, -(-D // 128), dtype=torch.uint8, device="meta"))
+    if D % 128 == 0:
+        gdn2.act_pack(x), gdn2.act_unpack(p)
+        return
+    with pytest.raises(ValueError, match="D"):
+        gdn2.act_pack(x)
+    with pytest.raises(ValueError, match="D"):
+        gdn2.act_unpack(p)
