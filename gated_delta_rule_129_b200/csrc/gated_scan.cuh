@@ -57,6 +57,7 @@ struct ScanArgs {
   int D, slabs;                 // channels of a token (a multiple of 64); D / 64
   int* status;                  // set by the launch itself, or by the plan that wrote chunk_off
   int timeout_code;             // stored there by a wait that gave up
+  unsigned long long wait_ns;   // after which a wait for a step's maps gives up
 };
 
 __device__ __forceinline__ void store_io2(float* p, float x, float y) {
@@ -127,14 +128,30 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
       : "=r"(ok) : "r"((uint32_t)__cvta_generic_to_shared(bar)), "r"(parity) : "memory");
   return ok != 0;
 }
-// Bounded: false after two seconds.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+// The rest of a thread's wait for a step's maps, at most a.wait_ns; false: it gave up
+// and the status word says so.  A thread that gave up waits no more (a single try
+// takes 4 us at most), sends no maps and arms no barrier, so one is armed only by a
+// thread that saw its phase before complete.  The cluster's other blocks then miss
+// this one's maps and give up too, their waits having begun about when this one's
+// did: a cluster takes about one limit longer than its walk, however many steps
+// that has, and leaves the outputs unspecified.
+__device__ __forceinline__ bool wait_longer(uint64_t* bar, uint32_t parity, const ScanArgs& a) {
   const uint64_t t0 = tc::global_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 15u) == 0 && tc::global_ns() - t0 > 2000000000ull) return false;
+    if ((it & 15u) == 0 && tc::global_ns() - t0 > a.wait_ns) break;
   }
+  atomicExch(a.status, a.timeout_code);
+  return false;
+}
+// The end of a cluster's walk: no block ends while others may still write to it.
+// Maps on their way to a block that gave up are not waited for: they get ample time
+// to land.
+__device__ __forceinline__ void end_cluster_walk(bool lost) {
+  cluster_sync();
+  if (!lost) return;
+  const uint64_t t0 = tc::global_ns();
+  while (tc::global_ns() - t0 < 100000ull) {}
 }
 
 // What a block walks: one sequence, one slab.
@@ -248,6 +265,7 @@ __global__ void __launch_bounds__(kScanThr, 2) gated_scan_fwd_kernel(const ScanA
   using Stage = ScanStageFwd<IO>;
   Stage* stages = reinterpret_cast<Stage*>(smem_raw);
   __shared__ __align__(128) ScanFwdMaps<IO> maps;
+  bool lost = false;                                     // a wait of this thread gave up
   const ScanSeq q = scan_seq(a, cl);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = CLUSTER ? (int)cluster_rank() : 0;
   const int ch = q.slab * kScanSlab + 2 * lane;
@@ -303,6 +321,7 @@ __global__ void __launch_bounds__(kScanThr, 2) gated_scan_fwd_kernel(const ScanA
   };
   // the chunk's map, from its warps' maps, to every block of the cluster
   const auto hand_out = [&](int s) {
+    if (CLUSTER && lost) return;
     if (CLUSTER && lane == 0) tc::mbar_arrive_expect_tx(&maps.arrived[s & 3], min(cl, q.chunks - s * cl) * 512u);
     if (s * cl + rank >= q.chunks) return;
     const float4 m0 = maps.warp[s & 1][0][lane];
@@ -320,7 +339,8 @@ __global__ void __launch_bounds__(kScanThr, 2) gated_scan_fwd_kernel(const ScanA
   };
   const auto finish = [&](int s, const float2 (&al)[R], const float2 (&u)[R]) {
     const int j = s * cl + rank, here = min(cl, q.chunks - s * cl);   // chunks of this step
-    if (CLUSTER && !mbar_wait_cluster(&maps.arrived[s & 3], (s >> 2) & 1)) atomicExch(a.status, a.timeout_code);
+    if (CLUSTER && !mbar_try_wait_cluster(&maps.arrived[s & 3], (s >> 2) & 1) && !lost)
+      lost = !wait_longer(&maps.arrived[s & 3], (s >> 2) & 1, a);
     float2 h = x;                                        // the state that enters the block's chunk
     for (int r = 0; r < here; ++r) {
       if (r == rank) h = x;
@@ -371,7 +391,7 @@ __global__ void __launch_bounds__(kScanThr, 2) gated_scan_fwd_kernel(const ScanA
     step(s, al[0], u[0], al[1], u[1]);
     if (s < steps) step(s + 1, al[1], u[1], al[0], u[0]);
   }
-  if (CLUSTER) cluster_sync();                            // no block ends while others may still write to it
+  if (CLUSTER) end_cluster_walk(lost);
 }
 
 // Maps are (A, A', H, H') of a lane's two channels.
@@ -395,6 +415,7 @@ __global__ void __launch_bounds__(kScanThr, 2) gated_scan_bwd_kernel(const ScanA
   Stage& st = *reinterpret_cast<Stage*>(smem_raw);
   __shared__ __align__(128) ScanBwdMaps maps;             // of the gradient's recurrence
   __shared__ float2 wh[kScanWarps][32];                  // H of the warps' maps of the states (A is the same)
+  bool lost = false;                                     // a wait of this thread gave up
   const ScanSeq q = scan_seq(a, cl);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = CLUSTER ? (int)cluster_rank() : 0;
   const int ch = q.slab * kScanSlab + 2 * lane;
@@ -459,8 +480,8 @@ __global__ void __launch_bounds__(kScanThr, 2) gated_scan_bwd_kernel(const ScanA
     maps.warp[warp][lane] = make_float4(A.x, A.y, Q.x, Q.y);
     wh[warp][lane] = H;
     __syncthreads();
-    if (CLUSTER && threadIdx.x == 0) tc::mbar_arrive_expect_tx(&maps.arrived[k & 1], here * 512u);
-    if (warp == 0 && j < q.chunks) {                     // the chunk's map, to every block of the cluster
+    if (CLUSTER && threadIdx.x == 0 && !lost) tc::mbar_arrive_expect_tx(&maps.arrived[k & 1], here * 512u);
+    if (warp == 0 && j < q.chunks && !lost) {                     // the chunk's map, to every block of the cluster
       const float4 m0 = maps.warp[NW - 1][lane];
       A = make_float2(m0.x, m0.y);
       Q = make_float2(m0.z, m0.w);
@@ -480,7 +501,8 @@ __global__ void __launch_bounds__(kScanThr, 2) gated_scan_bwd_kernel(const ScanA
     // hands out after it has finished step k.
     if (!CLUSTER) __syncthreads();
     fetch(s - 1);
-    if (CLUSTER && !mbar_wait_cluster(&maps.arrived[k & 1], (k >> 1) & 1)) atomicExch(a.status, a.timeout_code);
+    if (CLUSTER && !mbar_try_wait_cluster(&maps.arrived[k & 1], (k >> 1) & 1) && !lost)
+      lost = !wait_longer(&maps.arrived[k & 1], (k >> 1) & 1, a);
     float2 r2 = x;                                       // r that enters the block's chunk
     for (int r = here - 1; r >= 0; --r) {
       if (r == rank) r2 = x;
@@ -521,7 +543,7 @@ __global__ void __launch_bounds__(kScanThr, 2) gated_scan_bwd_kernel(const ScanA
     }
     if (j == 0 && warp == 0) store_io2(a.dh0 + sidx, r2.x, r2.y);
   }
-  if (CLUSTER) cluster_sync();                            // no block ends while others may still write to it
+  if (CLUSTER) end_cluster_walk(lost);
 }
 
 // One token of n channels (4 per thread), states in place.

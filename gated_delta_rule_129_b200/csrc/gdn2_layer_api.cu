@@ -231,6 +231,7 @@ int scan_cluster(const gdn2_desc* d, const ScanLayout& L, int most) {
 gdn2_status scan_plan(const gdn2_desc* d, const ScanLayout& L, const int32_t* cu, gdn2::ScanArgs* a, cudaStream_t s) {
   a->status = at<int32_t>(d->workspace, L.off_status);
   a->timeout_code = (int)GDN2_ERR_DEVICE_TIMEOUT;
+  a->wait_ns = 2000000000ull;
   a->map.cu = cu;
   a->map.N = L.N;
   a->map.T = d->T;
