@@ -934,8 +934,9 @@ def gated_scan_bwd(v, log_alpha, w, dO, h0=None, dhT=None, cu_seqlens=None, *, c
     """``gdn2_gated_scan_bwd``: gradients of :func:`gated_scan_fwd`'s ``(out,
     hT)`` contracted with ``dO`` (the shape and dtype of ``v``) and ``dhT``
     (``[N, H, dv]`` fp32 or None).  ``chunk_states`` as that call on the same
-    inputs left them; if not given they are computed again from ``h0``.
-    Returns a dict of fp32 tensors ``v, log_alpha, w`` and ``h0``."""
+    inputs left them; if not given they are computed again from ``h0`` (a
+    ``workspace`` that is given then holds the status of both calls, 0 if both
+    went well).  Returns a dict of fp32 tensors ``v, log_alpha, w`` and ``h0``."""
     torch = _torch()
     sizes, dev, sshape = _scan_args(v, log_alpha, w, cu_seqlens)
     f32 = torch.float32
@@ -944,11 +945,14 @@ def gated_scan_bwd(v, log_alpha, w, dO, h0=None, dhT=None, cu_seqlens=None, *, c
         _expect("h0", h0, sshape, f32, dev)
     if dhT is not None:
         _expect("dhT", dhT, sshape, f32, dev)
+    given = workspace is not None
     d, workspace = _scratch("gdn2_gated_scan_workspace_size", workspace, dev, *sizes)
     r = ctypes.byref(d)
+    again = None   # with the caller's workspace: that of the forward call, whose status word is to stay
     if chunk_states is None:
         chunk_states = gated_scan_chunk_states(v, cu_seqlens)
-        _call("gdn2_gated_scan_fwd", dev, r, v.data_ptr(), log_alpha.data_ptr(), w.data_ptr(),
+        d0, again = _scratch("gdn2_gated_scan_workspace_size", None, dev, *sizes) if given else (d, None)
+        _call("gdn2_gated_scan_fwd", dev, ctypes.byref(d0), v.data_ptr(), log_alpha.data_ptr(), w.data_ptr(),
               _addr(h0), _addr(cu_seqlens), None, None, _addr(chunk_states))
     else:
         _expect_states(chunk_states, v, cu_seqlens, dev)
@@ -956,6 +960,9 @@ def gated_scan_bwd(v, log_alpha, w, dO, h0=None, dhT=None, cu_seqlens=None, *, c
     g = dict(v=like(w), log_alpha=like(w), w=like(w), h0=w.new_empty(sshape))
     _call("gdn2_gated_scan_bwd", dev, r, v.data_ptr(), log_alpha.data_ptr(), w.data_ptr(),
           _addr(chunk_states), _addr(cu_seqlens), dO.data_ptr(), _addr(dhT), *map(_addr, g.values()))
+    if again is not None:
+        word = workspace.view(-1).view(torch.uint8)[:4].view(torch.int32)
+        torch.maximum(word, again[:4].view(torch.int32), out=word)
     return g
 
 

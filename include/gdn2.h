@@ -446,7 +446,8 @@ GDN2_API gdn2_status gdn2_token_epilogue_bwd(const gdn2_desc* desc, const void* 
  * desc->workspace: gdn2_gated_scan_workspace_size(desc) bytes, 256-byte
  * aligned; its first int32 is the status word: a malformed cu_seqlens stores
  * GDN2_ERR_SEQLENS there and leaves the outputs unspecified, a bounded wait that
- * gave up GDN2_ERR_DEVICE_TIMEOUT.
+ * gave up (after two seconds) GDN2_ERR_DEVICE_TIMEOUT, likewise.  Each call writes
+ * the word anew: copy it before the next call on the same workspace.
  * ------------------------------------------------------------------------ */
 GDN2_API size_t gdn2_gated_scan_workspace_size(const gdn2_desc* desc);
 

@@ -1,5 +1,6 @@
 """The binding's training calls on the CPU: what they hand to the library, and what they refuse.  No kernel runs; where a
 call has to get past its checks, the device check and the library call are stood in for."""
+import ctypes
 from types import SimpleNamespace
 
 import pytest
@@ -79,3 +80,33 @@ def test_checkpoints_refuse_rows_past_the_library(monkeypatch, D):
         gdn2.act_pack(x)
     with pytest.raises(ValueError, match="D"):
         gdn2.act_unpack(p)
+
+
+class _Library:
+    """Stands in for the scan's calls: each writes the status it is told to the workspace's first word."""
+
+    def __init__(self, monkeypatch, **status):
+        monkeypatch.setattr(gdn2, "_cuda_device", lambda name, t: t.device)
+        monkeypatch.setattr(gdn2, "_call", lambda where, device, desc, *a: self.call(where, desc._obj))
+        self.status, self.calls = status, []
+
+    def call(self, where, desc):
+        self.calls.append(where)
+        ctypes.c_int32.from_address(desc.workspace).value = self.status[where]
+
+
+@pytest.mark.parametrize("fwd,bwd,want", [(0, 0, 0), (8, 0, 8), (0, 8, 8), (5, 5, 5)])
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.float32])
+def test_backward_keeps_the_status_of_the_states_it_computes_again(monkeypatch, fwd, bwd, want, dtype):
+    lib = _Library(monkeypatch, gdn2_gated_scan_fwd=fwd, gdn2_gated_scan_bwd=bwd)
+    ws = torch.full((65536,), 77, dtype=dtype)
+    gdn2.gated_scan_bwd(_x(*T4), _x(*T4), _x(*T4), _x(*T4), workspace=ws)
+    assert lib.calls == ["gdn2_gated_scan_fwd", "gdn2_gated_scan_bwd"]
+    assert int(ws.view(torch.uint8)[:4].view(torch.int32)) == want
+
+
+def test_backward_from_kept_states_reports_its_own_status(monkeypatch):
+    _Library(monkeypatch, gdn2_gated_scan_bwd=0)
+    ws = torch.full((65536,), 77, dtype=torch.uint8)
+    gdn2.gated_scan_bwd(_x(*T4), _x(*T4), _x(*T4), _x(*T4), workspace=ws, chunk_states=_x(1, 2, 64))
+    assert int(ws[:4].view(torch.int32)) == 0

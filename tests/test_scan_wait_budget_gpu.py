@@ -114,3 +114,24 @@ def test_with_every_map_the_walk_is_the_librarys(probe, gdn2, io, cl):
     assert status == 0
     for a, n in zip(got, ("v", "log_alpha", "w", "h0")):
         assert torch.equal(a, g[n]), n
+
+
+@pytest.mark.gpu
+def test_status_of_a_backward_call_that_computes_the_states_again(gdn2):
+    """Its workspace's first word: 0, or the malformed cu_seqlens that both launches see; captured and replayed too."""
+    import torch
+    v, la, w, dO = _inputs(300, 128, torch.bfloat16)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    word = ws[:4].view(torch.int32)
+    for cu, want in (([0, 100, 300], 0), ([0, 100, 299], 5), ([0, 200, 100, 300], 5), (None, 0)):
+        t = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+        gdn2.gated_scan_bwd(v, la, w, dO, cu_seqlens=t, workspace=ws)
+        assert int(word) == want, cu
+    ref = gdn2.gated_scan_bwd(v, la, w, dO)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = gdn2.gated_scan_bwd(v, la, w, dO, workspace=ws)
+    word.fill_(99)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(word) == 0 and all(torch.equal(g[k], ref[k]) for k in ref)
