@@ -49,8 +49,10 @@ __device__ __forceinline__ void load_act(const XT* p, float power, float (&o)[PE
 }
 
 // The hardware's exponential, reciprocal and reciprocal square root on numbers
-// that flush to zero below 2^-126: one instruction each.  Relative errors of
-// some 2^-22; where exp(-u) leaves fp32's range the sigmoid is 0 or 1.
+// that flush to zero below 2^-126: one instruction each, within some 2^-22.  The
+// exponential's argument is rounded, so a sigmoid's relative error grows as
+// |u| 2^-24 for u < 0 (3e-6 at -50, of a value of 2e-22); where exp(-u) leaves
+// fp32's range the sigmoid is 0 or 1.
 __device__ __forceinline__ float ex2_ftz(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
 __device__ __forceinline__ float rcp_ftz(float x) { float y; asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
 __device__ __forceinline__ float rsqrt_ftz(float x) { float y; asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
@@ -58,6 +60,16 @@ __device__ __forceinline__ float2 sigmoid2(float2 u) {
   const float2 e = __fmul2_rn(u, make_float2(-1.44269504f, -1.44269504f));
   const float2 d = __fadd2_rn(make_float2(ex2_ftz(e.x), ex2_ftz(e.y)), make_float2(1.f, 1.f));
   return make_float2(rcp_ftz(d.x), rcp_ftz(d.y));
+}
+// sig(u) and 1 - sig(u), the latter as exp(-u) sig(u): the difference would lose all
+// digits where sig(u) is near 1 (4 % at u = 14).  (Where exp(-u) leaves fp32's
+// range sig(u) is 0, and so is their product.)
+__device__ __forceinline__ void sigmoids2(float2 u, float2& sg, float2& rest) {
+  const float2 t = __fmul2_rn(u, make_float2(-1.44269504f, -1.44269504f));
+  const float2 e = make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), d = __fadd2_rn(e, make_float2(1.f, 1.f));
+  constexpr float top = 8.5070592e37f;   // 2^126, whose reciprocal is not flushed to zero
+  sg = make_float2(rcp_ftz(d.x), rcp_ftz(d.y));
+  rest = __fmul2_rn(make_float2(fminf(e.x, top), fminf(e.y, top)), sg);
 }
 
 // A launch that adds up what the one before it left may begin while that one
@@ -458,11 +470,12 @@ __global__ void __launch_bounds__(kTokThreads, 4) token_epilogue_bwd_kernel(cons
     const long long next = r0 + stride;
     if (next < a.rows) load(next + r < a.rows ? next + r : next);
     float2 s2 = make_float2(0.f, 0.f), m2 = s2;
-    float2 sg[P];
+    float2 rest[P];                                          // 1 - sig(g)
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      sg[j] = sigmoid2(g[j]);
-      dy[j] = __fmul2_rn(dy[j], sg[j]);                      // dout sig(g)
+      float2 sg;
+      sigmoids2(g[j], sg, rest[j]);
+      dy[j] = __fmul2_rn(dy[j], sg);                         // dout sig(g)
       g[j] = __fmul2_rn(dy[j], wt[j]);                       // dn
       s2 = __ffma2_rn(o[j], o[j], s2);
       m2 = __ffma2_rn(g[j], o[j], m2);
@@ -475,14 +488,14 @@ __global__ void __launch_bounds__(kTokThreads, 4) token_epilogue_bwd_kernel(cons
     }
     // n = o rn; mean(dn n) = rn mean(dn o)
     const float rn = rsqrt_ftz(ss * (1.f / DV) + kTokEps), c = -rn * rn * (mm * (1.f / DV));
-    const float2 rn2 = make_float2(rn, rn), c2 = make_float2(c, c), one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
+    const float2 rn2 = make_float2(rn, rn), c2 = make_float2(c, c);
     const size_t at = (size_t)(r0 + r) * DV + l * kEpiBwdPer;
     float2 dg[P];
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const float2 n = __fmul2_rn(o[j], rn2);
       if (live) dw[j] = __ffma2_rn(dy[j], n, dw[j]);
-      dg[j] = __fmul2_rn(__fmul2_rn(g[j], n), __ffma2_rn(sg[j], minus, one));
+      dg[j] = __fmul2_rn(__fmul2_rn(g[j], n), rest[j]);
       g[j] = __fmul2_rn(rn2, __ffma2_rn(c2, o[j], g[j]));    // do
     }
     if (live) {
