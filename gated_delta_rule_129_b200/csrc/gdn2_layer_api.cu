@@ -138,7 +138,7 @@ gdn2_status pro_bwd_layout(const gdn2_desc* d, bool packed, int W, int bytes, Pr
 
 template <typename XT, typename IO, int D, int W>
 gdn2_status launch_pro_bwd_w(const gdn2::TokProBwdArgs& a, dim3 grid, cudaStream_t s) {
-  auto kern = gdn2::token_prologue_bwd_kernel<XT, IO, D, W, 2>;
+  auto kern = gdn2::token_prologue_bwd_kernel<XT, IO, D, W>;
   constexpr int smem = gdn2::pro_bwd_smem<XT>(D, W);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return GDN2_ERR_CUDA;
   kern<<<grid, gdn2::kBwdWarps * 32, smem, s>>>(a);

@@ -30,13 +30,13 @@ namespace gdn2 {
 template <typename XT, int PER>
 __device__ __forceinline__ void load_act(const XT* p, float power, float (&o)[PER]) {
   if constexpr (sizeof(XT) == 1) {
-    uint32_t w[(PER + 3) / 4];
-    if constexpr (PER == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
-    else if constexpr (PER == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
-    else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    static_assert(PER == 2 || PER == 4, "a lane's channels of 64 or 128");
+    uint32_t w;
+    if constexpr (PER == 2) w = *reinterpret_cast<const uint16_t*>(p);
+    else w = *reinterpret_cast<const uint32_t*>(p);
 #pragma unroll
     for (int i = 0; i < PER; i += 2) {
-      const float2 c = i % 4 == 0 ? code_values<0>(w[i / 4], power) : code_values<2>(w[i / 4], power);
+      const float2 c = i == 0 ? code_values<0>(w, power) : code_values<2>(w, power);
       o[i] = c.x;
       o[i + 1] = c.y;
     }
@@ -99,6 +99,8 @@ constexpr int kBwdStages = 2;
 // take 16 W + 8 (W + 3) of them at d = 128, wider rows a few more.  At W = 4 bf16
 // rows spill with four blocks (164 us against 159 us with three), 8-bit rows do not
 // (164 us against 172 us); at W = 3 four are better for both (147 us against 157 us).
+// (Measured at d = 128.  The counts are the same at d = 64, whose lanes hold half as much:
+// there one block more would fit for bf16 and fp32 rows at W = 4, for all at W = 7 and 8.)
 __host__ __device__ constexpr int pro_bwd_blocks(int bytes, int W) {
   return W <= 3 ? (bytes == 4 ? 3 : 4) : W == 4 ? (bytes == 1 ? 4 : 3) : W <= 6 ? 3 : 2;
 }
@@ -137,14 +139,15 @@ __device__ __forceinline__ void warp_sums(float (&v)[NV]) {
 }
 
 // grid: (token groups, H, projections).  A warp walks one run of consecutive
-// tokens of one head of one projection, G tokens at a time, and W - 1 more on
+// tokens of one head of one projection, two tokens (G) at a time, and W - 1 more on
 // either side; a block's warps have neighbouring runs.  Rows arrive through the
 // warp's own ring in shared memory (asynchronous copies, no block barrier).  The
 // window of x and the gradients that still wait for later tokens stay in
 // registers, and so do the tap gradients, over the whole run.
-template <typename XT, typename IO, int D, int W, int G>
+template <typename XT, typename IO, int D, int W>
 __global__ void __launch_bounds__(kBwdWarps * 32, pro_bwd_blocks(sizeof(XT), W)) token_prologue_bwd_kernel(const TokProBwdArgs a) {
-  static_assert(kBwdStage == 8 && (G == 2 || G == 4), "groups of a stage");
+  constexpr int G = 2;
+  static_assert(kBwdStage == 4 * G, "four groups a stage");
   constexpr int PER = D / 32, NP = PER / 2;
   constexpr int ROWX = D * (int)sizeof(XT), ROWG = D * 4, STAGE = kBwdStage * (ROWX + ROWG);
   extern __shared__ __align__(16) uint8_t smem[];
@@ -331,9 +334,9 @@ __global__ void __launch_bounds__(kBwdWarps * 32, pro_bwd_blocks(sizeof(XT), W))
       // inside: full windows of the sequence at hand, every row that is completed the run's own
       const auto stage = [&](auto edge) {
         group(edge, std::integral_constant<int, 0>{}, t, st, pd, pbase);
-        if constexpr (G <= 2) group(edge, std::integral_constant<int, 2>{}, t, st, pd, pbase);
-        group(edge, std::integral_constant<int, 4>{}, t, st, pd, pbase);
-        if constexpr (G <= 2) group(edge, std::integral_constant<int, 6>{}, t, st, pd, pbase);
+        group(edge, std::integral_constant<int, G>{}, t, st, pd, pbase);
+        group(edge, std::integral_constant<int, 2 * G>{}, t, st, pd, pbase);
+        group(edge, std::integral_constant<int, 3 * G>{}, t, st, pd, pbase);
       };
       if (t - (W - 1) >= ts && t + kBwdStage <= min(own, s1) && t - s0 >= W - 1) stage(std::false_type{});
       else stage(std::true_type{});
