@@ -42,3 +42,28 @@ def test_large_rows(gdn2, d, W, scale, every, io, dy_scale):
         # sums over 60 tokens: 60 * 2^-24 more
         off = (got["conv_" + c].double() - dtap).reshape(H, d, W).norm(dim=1)
         assert bool((off <= (C + 60 * 2.0 ** -24) * tap_bound).all()), c
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [1e-20, 1e-3, 1e6, 1e12, 1e15, 1e18])
+def test_epilogue_large_and_small_rows(gdn2, scale, d, io):
+    """The RMS norm's backward: do within C of r |dn| (row sums of two times, the root, six roundings: as the prologue's
+    rows), at every scale whose sum of squares fits fp32 and down to rows that the eps outweighs."""
+    import torch
+    dt = torch.float32 if io == "f32" else torch.bfloat16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    rows = torch.where(torch.arange(40, device="cuda") % 3 == 0, scale, 1.0).reshape(1, 40, 1, 1)
+    o, gate, dout = (n(1, 40, 3, d) * rows).to(dt), n(1, 40, 3, d).to(dt), n(1, 40, 3, d).to(dt)
+    wt = torch.rand(d, generator=g, device="cuda") + 0.5
+    got = gdn2.token_epilogue_bwd(o, gate, wt, dout)
+    x, sig = o.double(), torch.sigmoid(gate.double())
+    r = 1 / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6)
+    y, dn = x * r, dout.double() * wt.double() * sig
+    half = 2.0 ** -8 if io == "bf16" else 0.0
+    for name, ref, scale_of in (("o", r * (dn - y * (y * dn).mean(-1, keepdim=True)), r[..., 0] * dn.norm(dim=-1)),
+                                ("gate", dn * y * (1 - sig), (dn * y).norm(dim=-1))):
+        off = (got[name].double() - ref).norm(dim=-1) - half * ref.norm(dim=-1)
+        assert (off / scale_of).max().item() <= C, name
