@@ -681,15 +681,13 @@ def _blocks(d):
     return (d + 127) // 128
 
 
-def _rows_cols(name, t):
+def _long_rows(name, t):
     """``t``'s rows and their length for the library, whose rows are under 2^31
     values long: rows of whole blocks go as rows of one block, stored alike."""
     D = t.shape[-1]
-    if D % 128 == 0:
-        return t.numel() // 128, 128
-    if D > 0x7fffffff:
+    if D % 128 != 0:
         raise ValueError(f"{name} has rows of D = {D} values; past 2^31 D must be a multiple of 128")
-    return t.numel() // D, D
+    return t.numel() // 128, 128
 
 
 @_on_stream
@@ -703,8 +701,9 @@ def act_pack(x, *, out=None):
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"x must have shape [..., D] with D >= 1, got {tuple(x.shape)}")
     _need_contig(x)
-    rows, cols = _rows_cols("x", x)
-    eshape = (*x.shape[:-1], _blocks(x.shape[-1]))
+    D = x.shape[-1]
+    rows, cols = (x.numel() // D, D) if D < 1 << 31 else _long_rows("x", x)
+    eshape = (*x.shape[:-1], _blocks(D))
     if out is None:
         out = PackedAct(torch.empty_like(x, dtype=torch.int8), torch.empty(eshape, dtype=torch.uint8, device=dev))
     else:
@@ -727,7 +726,7 @@ def act_unpack(packed, dtype=None, *, out=None):
     D = codes.shape[-1]
     _expect("codes", codes, codes.shape, torch.int8, dev)
     _expect("exps", exps, (*codes.shape[:-1], _blocks(D)), torch.uint8, dev)
-    rows, cols = _rows_cols("codes", codes)
+    rows, cols = (codes.numel() // D, D) if D < 1 << 31 else _long_rows("codes", codes)
     dtype = dtype if dtype is not None else torch.bfloat16 if out is None else out.dtype
     io = _io(dtype)
     if out is None:
@@ -901,7 +900,9 @@ def gated_scan_fwd(v, log_alpha, w, h0=None, cu_seqlens=None, *, out=None, hT=No
     ``v`` is float32 or bfloat16 ``[B, T, H, dv]``, ``log_alpha`` and ``w``
     float32 of that shape, ``h0`` float32 ``[N, H, dv]`` or None; ``chunk_states``
     (:func:`gated_scan_chunk_states`) receives the state at the start of every
-    64-token chunk, for :func:`gated_scan_bwd`."""
+    64-token chunk, for :func:`gated_scan_bwd`.  A malformed ``cu_seqlens`` (and a
+    device wait that gave up) leaves the outputs unspecified and a status other
+    than 0 in the first int32 of a ``workspace`` that is given."""
     torch = _torch()
     sizes, dev, sshape = _scan_args(v, log_alpha, w, cu_seqlens)
     f32 = torch.float32

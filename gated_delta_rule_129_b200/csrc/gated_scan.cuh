@@ -25,12 +25,12 @@
 // with one another, so neither CL nor the packing changes a bit of the results.
 //
 // Measured, 16 heads of 128, bf16: forward 16K x 1 (CL = 8) 72 us, 2K x 8 (CL = 1)
-// 66 us, 85 % and 92 % of the measured copy bandwidth; backward 141 and 148 us,
-// 87 % and 83 %; 32 packed sequences of 256 to 8192 tokens 100 % and 94 %: once
+// 66 us, 85 % and 92 % of the measured copy bandwidth; backward 140 and 147 us,
+// 87 % and 84 %; 32 packed sequences of 256 to 8192 tokens 100 % and 94 %: once
 // blocks come and go on their own, waits no longer coincide.  A single pass that looked back over published tiles instead of walking
 // took 202 us forward (160 KB of registers an SM in flight over 14 us waits); one
 // thread per channel 9.3 ms.  With few channels a step's length bounds it: 16K x 1
-// with 256 channels 52 us, 32 steps of 1.6 us.
+// with 256 channels 46 to 54 us (by the GPU), 32 steps of 1.4 to 1.7 us.
 #pragma once
 
 #include "common.cuh"

@@ -93,14 +93,15 @@ gdn2_status check_pack(long long rows, int cols, gdn2_io_dtype io, const void* x
 // Blocks along the tokens in the prologue's backward pass.  A block's work does
 // not depend on how many there are, so the best count fills whole waves of
 // blocks: up to four waves, the count that leaves the least of the last wave
-// empty, the fewest blocks among equals; runs of 16 tokens at least, so that the
-// W - 1 tokens a warp walks on either side stay few.
+// empty, the fewest blocks among equals; and no more than one block for each 64
+// tokens begun, so that the W - 1 tokens a warp walks on either side stay few: where
+// that limit binds, a warp's run is 9 to 16 tokens (fewer under 65 tokens in all).
 constexpr int kProBwdSms = 148;   // B200
-constexpr int kProBwdMinRun = 16;
+constexpr int kProBwdRun = 16;   // tokens of a warp's run at that limit, at most
 constexpr int kEpiBwdBlocks = 148 * 4;   // four blocks an SM, each walking rows with a stride
 
 int pro_groups(long long tokens, int rows /* heads times projections of the launch */, int slots) {
-  const long long most = std::max<long long>(1, (tokens + gdn2::kBwdWarps * kProBwdMinRun - 1) / (gdn2::kBwdWarps * kProBwdMinRun));
+  const long long most = std::max<long long>(1, (tokens + gdn2::kBwdWarps * kProBwdRun - 1) / (gdn2::kBwdWarps * kProBwdRun));
   long long best = 1;
   double best_fill = 0;
   for (int waves = 1; waves <= 4; ++waves) {
