@@ -19,10 +19,10 @@
 //
 // The floor of both directions is HBM traffic (3 bytes a value in bf16).  For rows of
 // whole blocks unpacking is near it (16K x 16 rows of 128, bf16: 17 us of 15.4;
-// fp32 29 us of 25.6); packing is bound by its instructions (23 us, fp32 36 us: 0.74
-// issues a cycle with DRAM at 40 %), as are both directions of rows that are not a
-// multiple of four values, whose accesses are single values.  A block
-// belongs to a group of lanes, the fewest that hold it at LV values a lane (8
+// fp32 29 us of 25.6); packing is bound by its instructions (23 us, fp32 37 us: 0.74
+// issues a cycle with DRAM at 40 %).  Rows that are not whole blocks take more and
+// narrower accesses, single values where their length is odd (17 to 55 % of HBM).
+// A block belongs to a group of lanes, the fewest that hold it at LV values a lane (8
 // bf16 or 4 fp32 values: 16 bytes), so that short rows fill their warps too; a
 // thread has its kPackPasses blocks' values in flight together.  Rows whose
 // length is a multiple of 128 are blocks one after the other and need no row
